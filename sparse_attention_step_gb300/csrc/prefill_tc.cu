@@ -115,15 +115,24 @@ struct E8Tail {
   alignas(16) float ks[kScaleStages][2][kScaleRow];
   float vs[kScaleStages][2][kScaleRow];
   float lv[kScaleStages][2][kScaleRow];  // log2 |vs|; -inf for 0 and for what is not finite (so whatever the reference)
+  float room;                      // weight_room of the unit's blocks
   float vmax[kScaleStages][2][2];  // the largest finite |V scale| of a block's halves
   alignas(16) float raw[kCodeSlots][2][kBlock];  // as loaded: K's, V's
 };
-// Weights at a new reference are at most 2^0: exact to half a step down to 2^-14 of
-// the largest, off by 2^-25 of it below. Until it moves, the sum of a block's may
-// grow to 2^15 (times the largest V scale), which fp16 surely holds. A reference 2^5
-// nearer to that moved often where scores spread over many bits: with a standard
-// deviation of 4 bits 1064 us, 2^2 nearer 936, this 846.
-constexpr float kPairWeightBits = 0.f;
+// Weights at a new reference are at most 2^room: exact to half a step down to 2^-14,
+// off by 2^-25 below it, so by 2^-(25 + room) of the largest weight. Each of n tokens may
+// lose that: the room grows with the number of blocks, so that a row loses at most n
+// 2^-(25 + room) <= 2^-12 of its largest weight, up to 2^28 tokens (the room ends at
+// the bound below). Until the reference moves, the sum of a block's may
+// grow to 2^15 (times the largest V scale), which fp16 surely holds. More room than that
+// makes the reference move often where scores spread over many bits: 33 blocks, a
+// standard deviation of 4 bits, room 5 1064 us, 2 936, 0 846.
+constexpr int kRoomBlocks = 7;  // no room up to 2^7 blocks
+constexpr int kMaxRoom = 15;
+__device__ inline float weight_room(int nblk) {
+  const int log2_blocks = nblk > 1 ? 32 - __clz(nblk - 1) : 0;  // rounded up
+  return static_cast<float>(min(max(log2_blocks - kRoomBlocks, 0), kMaxRoom));
+}
 constexpr float kWeightTop = 32768.f;
 constexpr float kSumBits = 90.f;           // l: at most 2^90 a term at a new reference,
 constexpr float kSumTop = 1.26765060e30f;  // 2^100 a block after
@@ -275,6 +284,7 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
     if (lane == 0) {
       st.n_blocks = n;
       st.abort = 0;
+      if constexpr (kE8) e8.room = weight_room(n);
     }
   }
   if (warp == kMmaWarp) {
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
           Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, 16));
           const int any_half = __shfl_xor_sync(0xffffffffu, static_cast<int>(over), 16) | static_cast<int>(over);
           if (any_half) {
-            const float ref = fmaxf(m, fmaxf(Mx - kPairWeightBits, mx - kSumBits));
+            const float ref = fmaxf(m, fmaxf(Mx - e8.room, mx - kSumBits));
             grow = ex2_approx(m - ref);
             l *= grow;
             m = ref;
