@@ -277,8 +277,8 @@ msa_status msa_sparse_attn_decode(const void* q, int32_t num_q_heads, const msa_
  * longer list is cut there and the device status records MSA_ERR_UNSUPPORTED.
  * The rows of the chunk's own tokens have to be finite: a later token's key and
  * scales do not reach an earlier query, but a NaN or an infinity among its values
- * may, in the block that both lie in. (e4m3: tokens from seq_lens on are left out,
- * whatever their rows hold.)
+ * may, in the block that both lie in. kv->seq_lens is not read: the tokens up to the
+ * chunk's end are taken as present, whether the lengths count them yet or not.
  * e4m3: the weight of a token (its softmax weight times its V scale) is rounded to 11
  * bits, or, where it is small against the row's largest, to a multiple of a fixed fraction of
  * that, such that the roundings of all small weights of a row add up to at most 2^-12 of the

@@ -44,7 +44,6 @@ __global__ void __launch_bounds__(kPfThreads) prefill_bf16_kernel(const __grid_c
   const int seq = a.batch.seq_of_tile(tile);
   const int jt = tile - a.batch.tile_off[seq];  // tile within its sequence
   const int64_t q_start = a.batch.q_start[seq];
-  const int64_t len = kv.seq_len(seq, a.status, kIdPrefill);
   const int64_t diag = q_start / kBlock + jt;
 
   if (warp == 0) {
@@ -163,7 +162,7 @@ __global__ void __launch_bounds__(kPfThreads) prefill_bf16_kernel(const __grid_c
     }
     // mask and scale
     const int64_t key0 = static_cast<int64_t>(b) * kBlock;
-    const bool need_mask = (key0 + kBlock - 1 > diag * kBlock) || (key0 + kBlock > len);
+    const bool need_mask = key0 + kBlock - 1 > diag * kBlock;
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
@@ -173,7 +172,7 @@ __global__ void __launch_bounds__(kPfThreads) prefill_bf16_kernel(const __grid_c
         float z = sc[nt][e] * a.scale_log2;
         if (need_mask || !live[hr]) {
           const int64_t kp = key0 + 8 * nt + 2 * c + (e & 1);
-          if (!live[hr] || kp > pos[hr] || kp >= len) z = -INFINITY;
+          if (!live[hr] || kp > pos[hr]) z = -INFINITY;
         }
         sc[nt][e] = z;
         mx[hr] = fmaxf(mx[hr], z);

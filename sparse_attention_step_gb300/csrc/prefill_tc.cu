@@ -44,7 +44,7 @@
 // near the largest score plus log2 |V's scale|: weights go to fp16 as 2^(x - R) vs,
 // l sums 2^(x - R), which fp32 holds whatever the scales. No maximum is taken
 // unless it is needed: the sum of the weights before their scales, times the
-// block's largest |V scale|, bounds them. Rows past the sequence's end are widened
+// block's largest |V scale|, bounds them. Rows past the chunk's end are widened
 // to zeros, their scales are staged as zeros and their scores masked.
 // Registers: 6 warpgroups x 80 are split by setmaxnreg into 4 (softmax) x 88 + 2 x
 // 64, where nothing spills. Groups below 8 leave rows idle: a token's rows are 4 (G <=
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
   if (kE8 && warp == kProducerWarp) {
     // ------------------------------------------------------------ producer of codes
     // tiles in the order K, K, V, V of a pair; rows of the next 32 blocks are looked up by the lanes
-    const int64_t len = kv.seq_len(seq, a.status, kIdPrefill);
+    const int64_t len = a.batch.q_start[seq] + a.batch.q_cnt[seq];  // the chunk's end: rows past it are left out
     int64_t row_l = -1;
     int32_t valid_l = 0;
     int n = 0;  // tiles issued
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
         row_l = -1;
         if (e < nblk) {
           const int64_t b = dense ? e : st.blocks[e];
-          if (b * kBlock < len) row_l = kv.block_row(seq, h, b, a.status, kIdPrefill);
+          row_l = kv.block_row(seq, h, b, a.status, kIdPrefill);
           valid_l = row_l < 0 ? 0 : static_cast<int32_t>(min(static_cast<int64_t>(kBlock), len - b * kBlock));
         }
       }
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
         ok = __all_sync(0xffffffffu, ok && wait_or_abort(&e8.scale_full[sst], (i / kScaleStages) & 1, abort, a.status));
         const bool take = ok && have;
         const int b = !have ? -1 : dense ? 2 * i + hf : st.blocks[2 * i + hf];
-        // last key of the block that the row sees: causal, and inside the sequence
+        // last key of the block that the row sees: causal, and before the chunk's end
         const int last = have ? min(b == diag ? tt : kBlock - 1, e8.valid[sst][hf] - 1) : kBlock - 1;
         const float4* kf = reinterpret_cast<const float4*>(e8.ks[sst][hf]);
         const float4* vf = reinterpret_cast<const float4*>(e8.vs[sst][hf]);
