@@ -666,8 +666,17 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
           }
           const float2 acc = fadd2(acc0, acc1);
           sum = acc.x + acc.y;
-          const bool over = take && live && !(sum * vmax <= kWeightTop && sum <= kSumTop);
+          bool over = take && live && !(sum * vmax <= kWeightTop && sum <= kSumTop);
           if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
+          if (over && b == diag) {  // with the largest V scale that the row sees: a later token's moves nothing
+            float seen = 0.f;
+#pragma unroll 1
+            for (int c = 0; c <= last; ++c) {
+              const float v = fabsf(e8.vs[sst][hf][c]);
+              if (v <= FLT_MAX) seen = fmaxf(seen, v);
+            }
+            over = !(sum * seen <= kWeightTop && sum <= kSumTop);
+          }
           float mx = -INFINITY, Mx = -INFINITY;  // largest score, and score plus log2 |V's scale|
 #pragma unroll 1
           for (int part = 0; part < 4; ++part) {
