@@ -36,9 +36,8 @@
  *     and sets a sticky status word in the workspace, read with
  *     msa_read_device_status.
  *   - Head dimension D = 128 and block size 64 are the only supported values.
- *   - The rows of a bf16 cache past a sequence's length, in its last block, are
- *     read and weighted by 0: they must be finite (zero-fill a cache once; rows
- *     left by earlier sequences are fine). fp32 and e4m3 caches have no such rule.
+ *   - Rows of k and v past a sequence's length (in a prefill: past its chunk's end) may
+ *     hold anything, NaN and infinities among it.
  *   - q, out, k, v, their scales and the pooled keys are moved in 16-byte pieces (vector
  *     loads and stores, asynchronous and tensor-memory-access copies): their
  *     base addresses must be 16-byte aligned (MSA_ERR_INVALID_ARG otherwise).
@@ -83,7 +82,7 @@ typedef enum msa_status {
  * token) has an fp32 scale >= 0 in k_scale / v_scale: element = code * scale.
  * q, out and the pooled keys of such a cache are bf16. Read by pooling,
  * selection, sparse and dense decode, the decode step and the prefill attention.
- * Rows and scales past a sequence's length may hold anything. */
+ * Scales past a sequence's length may hold anything, as rows may. */
 typedef enum msa_dtype { MSA_DTYPE_F32 = 0, MSA_DTYPE_BF16 = 1, MSA_DTYPE_E4M3 = 2 } msa_dtype;
 typedef enum msa_kv_layout { MSA_KV_CONTIGUOUS = 0, MSA_KV_PAGED = 1 } msa_kv_layout;
 

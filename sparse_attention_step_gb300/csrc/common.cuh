@@ -216,6 +216,17 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {
 __device__ inline uint32_t swz128(int row, int chunk) {
   return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
+// Rows [first, end) of a 64 x 128 bf16 tile in shared memory (two boxes of 64 columns, box_stride
+// bytes apart, rows of 128 bytes whatever their swizzle) set to zero by threads 0 .. n - 1. A row of V that no
+// token owns has weight 0, but 0 times what an earlier owner of the page left there may be NaN. The rows
+// were written, and will be overwritten, by TMA copies: the fence orders these writes with them.
+__device__ inline void zero_tile_rows(uint8_t* tile, int box_stride, int first, int end, int thread, int n) {
+#pragma unroll 1
+  for (int i = 16 * first + thread; i < 16 * end; i += n)
+    *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * box_stride + (i >> 4) * 128 + (i & 7) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async();
+}
 
 __device__ inline float bf16_bits_to_f32(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 

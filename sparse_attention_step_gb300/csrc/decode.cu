@@ -115,8 +115,15 @@ __global__ void __launch_bounds__(kDecThreads) decode_bf16_kernel(const __grid_c
         ldsm_x4(kbase + (kk >> 2) * 8192 + swz128(krow, (kk & 3) * 2 + kchunk), a0, a1, a2, a3);
         mma_bf16(sacc, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
       }
-      const int64_t tok = static_cast<int64_t>(a.idx ? st.blocks[i] : st.dense_lo + i) * kBlock + 16 * warp + g;
+      const int64_t first = static_cast<int64_t>(a.idx ? st.blocks[i] : st.dense_lo + i) * kBlock + 16 * warp;
+      const int64_t tok = first + g;
       const bool v0 = tok < len, v1 = tok + 8 < len;
+      if (first + 16 > len) {  // this warp alone reads its 16 rows of V
+        const int64_t left = len - first;
+        zero_tile_rows(ring + stg * kStageBytes + 16384, 8192, 16 * warp + (left > 0 ? static_cast<int>(left) : 0),
+                       16 * warp + 16, lane, 32);
+        __syncwarp();
+      }
       const float s0 = v0 ? sacc[0] * a.scale_log2 : -INFINITY;  // token g,   head 2c
       const float s1 = v0 ? sacc[1] * a.scale_log2 : -INFINITY;  // token g,   head 2c+1
       const float s2 = v1 ? sacc[2] * a.scale_log2 : -INFINITY;  // token g+8, head 2c

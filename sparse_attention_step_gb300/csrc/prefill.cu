@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(kPfThreads) prefill_bf16_kernel(const __grid_c
   const int jt = tile - a.batch.tile_off[seq];  // tile within its sequence
   const int64_t q_start = a.batch.q_start[seq];
   const int64_t diag = q_start / kBlock + jt;
+  const int64_t tail = q_start + a.batch.q_cnt[seq] - diag * kBlock;  // the chunk's end, from the diagonal block on
 
   if (warp == 0) {
     // the valid entries of the unit's list, in order, read 32 at a time
@@ -146,6 +147,12 @@ __global__ void __launch_bounds__(kPfThreads) prefill_bf16_kernel(const __grid_c
     const int b = dense ? i : st.blocks[i];
     const uint32_t kbase = smem_u32(ring + stg * kPfStageBytes);
     const uint32_t vbase = kbase + 16384;
+    if (b == diag && tail < kBlock) {
+      // rows of V past the chunk's end: every warp writes the same zeros before it reads them (a barrier
+      // would hang the others where one warp's wait gave up), and no stage is refilled before all have
+      zero_tile_rows(ring + stg * kPfStageBytes + 16384, 8192, static_cast<int>(tail), kBlock, lane, 32);
+      __syncwarp();
+    }
     float sc[8][4];
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;

@@ -79,6 +79,8 @@ constexpr int kRingBytes = kTcStages * kPairBytes;
 constexpr int kMaxList = 512;
 constexpr float kRescaleLog2 = 8.0f;  // lazy rescale threshold (factor 256)
 
+__device__ uint4 g_zero_rows[kBlock * 128 / 16];  // 64 rows of half a head, never written
+
 struct TcTail {
   uint64_t q_full;
   uint64_t k_full[kTcStages];
@@ -89,9 +91,12 @@ struct TcTail {
   uint64_t p_full[kTcTiles];
   uint64_t o_final[kTcTiles];
   uint64_t drain;
+  uint64_t cut_full;  // V of the pair with the chunk's end, before its rows past that are cleared
   uint32_t tmem_base;
   int32_t n_blocks;
   int32_t abort;
+  int32_t cut_at;   // where the list has the block in which the chunk ends, or -1 (bf16 caches); ...
+  int32_t cut_row;  // ... the block's rows from here on are no token's
   int32_t blocks[kMaxList];
 };
 
@@ -239,6 +244,7 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
       mbar_init(&st.o_final[t], 1);
     }
     mbar_init(&st.drain, 1);
+    mbar_init(&st.cut_full, 1);
     if constexpr (kE8) {
       for (int i = 0; i < kCodeSlots; ++i) {
         mbar_init(&e8.code_full[i], 1);
@@ -262,7 +268,9 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
   }
   if (warp == 0) {
     // the valid entries of the unit's list, in order, read 32 at a time
-    int n = 0;
+    const int tail = static_cast<int>(a.batch.q_start[seq] + a.batch.q_cnt[seq] - diag * kBlock);
+    const bool ends = !kE8 && tail < kBlock;  // the chunk, in the diagonal block
+    int n = 0, at = -1;
     if (a.idx != nullptr) {
       const int32_t* list = a.idx + (static_cast<int64_t>(tile) * a.hkv + h) * a.k_total;
       for (int base = 0; base < a.k_total; base += 32) {
@@ -272,6 +280,10 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
         const uint32_t ballot = __ballot_sync(0xffffffffu, keep);
         const int pos = n + __popc(ballot & ((1u << lane) - 1u));
         if (keep && pos < kMaxList) st.blocks[pos] = b;
+        if (ends) {
+          const uint32_t here = __ballot_sync(0xffffffffu, b == diag);
+          if (here != 0) at = n + __popc(ballot & ((here & (0u - here)) - 1u));
+        }
         n += __popc(ballot);
       }
       if (n > kMaxList) {  // more valid entries than the kernel holds
@@ -280,9 +292,12 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
       }
     } else {
       n = static_cast<int>(diag + 1);
+      if (ends) at = n - 1;
     }
     if (lane == 0) {
       st.n_blocks = n;
+      st.cut_at = at;
+      st.cut_row = tail;
       st.abort = 0;
       if constexpr (kE8) e8.room = weight_room(n);
     }
@@ -408,6 +423,8 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       int issued_k = 0, issued_v = 0;
+      const int cut_pair = st.cut_at >> 1;
+      bool cut_issued = false;
       for (int i = 0; i < npair; ++i) {
         const int stg = i % kTcStages, use = i / kTcStages, nb = blocks_in(i);
         auto row_of = [&](int j) {
@@ -424,10 +441,26 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
             tma_load_2d(ks + stg * kPairBytes + hd * 16384 + j * 8192, &tmk, 64 * hd, j ? y1 : y0, &st.k_full[stg]);
         issued_k = i + 1;
         if (i >= kTcStages && !wait_or_abort(&st.v_empty[stg], (use - 1) & 1, abort, a.status)) break;
-        mbar_arrive_expect_tx(&st.v_full[stg], nb * 16384);
-        for (int j = 0; j < nb; ++j)
+        auto load_v = [&](uint64_t* full) {
+          mbar_arrive_expect_tx(full, nb * 16384);
+          for (int j = 0; j < nb; ++j)
+            for (int hd = 0; hd < 2; ++hd)
+              tma_load_2d(vs + stg * kPairBytes + hd * 16384 + j * 8192, &tmv, 64 * hd, j ? y1 : y0, full);
+        };
+        if (i != cut_pair) {
+          load_v(&st.v_full[stg]);
+        } else {
+          // rows of V past the chunk's end are no token's: their weights are 0, but 0 times what an earlier owner
+          // of the page left there may be NaN, so zeros follow once the tiles have landed
+          load_v(&st.cut_full);
+          cut_issued = true;
+          if (!wait_or_abort(&st.cut_full, 0, abort, a.status)) break;
+          const uint32_t bytes = (kBlock - st.cut_row) * 128;
+          mbar_arrive_expect_tx(&st.v_full[stg], 2 * bytes);
           for (int hd = 0; hd < 2; ++hd)
-            tma_load_2d(vs + stg * kPairBytes + hd * 16384 + j * 8192, &tmv, 64 * hd, j ? y1 : y0, &st.v_full[stg]);
+            bulk_load(vs + stg * kPairBytes + hd * 16384 + (st.cut_at & 1) * 8192 + st.cut_row * 128, g_zero_rows,
+                      bytes, &st.v_full[stg]);
+        }
         issued_v = i + 1;
       }
       // The CTA that starts when this one ends is, in the dispatch order, one
@@ -461,6 +494,7 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
       }
       // drain: every load this thread issued has landed before the CTA may exit
       mbar_wait(&st.q_full, 0, a.status, kIdPrefill);
+      if (cut_issued) mbar_wait(&st.cut_full, 0, a.status, kIdPrefill);
       for (int i = issued_k - kTcStages < 0 ? 0 : issued_k - kTcStages; i < issued_k; ++i)
         mbar_wait(&st.k_full[i % kTcStages], (i / kTcStages) & 1, a.status, kIdPrefill);
       for (int i = issued_v - kTcStages < 0 ? 0 : issued_v - kTcStages; i < issued_v; ++i)

@@ -540,8 +540,15 @@ __global__ void __launch_bounds__(kStThreads, 2) decode_step_kernel(const __grid
         ldsm_x4(kbase + (kk2 >> 2) * 8192 + swz128(krow, (kk2 & 3) * 2 + kchunk), a0, a1, a2, a3);
         mma_bf16(sacc, a0, a1, a2, a3, qb[kk2][0], qb[kk2][1]);
       }
-      const int64_t tok = static_cast<int64_t>(slice_at(lo + i)) * kBlock + 16 * wq + g;
+      const int64_t first = static_cast<int64_t>(slice_at(lo + i)) * kBlock + 16 * wq;
+      const int64_t tok = first + g;
       const bool v0 = tok < len, v1 = tok + 8 < len;
+      if (first + 16 > len) {  // this warp alone reads its 16 rows of V
+        const int64_t left = len - first;
+        zero_tile_rows(ring + slot * kStStage + 16384, 8192, 16 * wq + (left > 0 ? static_cast<int>(left) : 0),
+                       16 * wq + 16, lane, 32);
+        __syncwarp();
+      }
       const float s0 = v0 ? sacc[0] * a.scale_log2 : -INFINITY;
       const float s1 = v0 ? sacc[1] * a.scale_log2 : -INFINITY;
       const float s2 = v1 ? sacc[2] * a.scale_log2 : -INFINITY;
