@@ -441,7 +441,8 @@ msa_status msa_trim_sequences(const msa_kv_desc* kv /* host */, const int32_t* k
  *   (a, b) -> (a cos - b sin, b cos + a sin), angle positions[t] * inv_freq[i],
  *   for the pairs i < rotary_dim/2 of the head's leading rotary_dim dims
  *   (cfg->interleaved says which two elements pair i holds).
- * Angles are exact to 2^-24 of half a turn at any position. Query heads go to q_out, key
+ * Angles are exact to 2^-24 of half a turn at any position and for any finite inv_freq.
+ * Query heads go to q_out, key
  * heads and value heads (unchanged) to the cache rows of slots[t]: row
  * slot % W of head h of run slot / W, W = max_tokens (contiguous; the run is the
  * sequence) or 64 (paged; the page). An e4m3 cache gets, per row, scale =

@@ -29,10 +29,10 @@
 //
 // Angles: fp32 products lose a far token's angle (at position 2^20 an fp32
 // angle of 1 rad per token is off by 0.06 rad). inv_freq / 2 pi is taken once
-// a lane as a 64-bit fixed-point fraction of a turn (24-bit mantissa times
-// 1 / 2 pi to 64 bits, in integers), position times it wraps modulo one turn
+// a thread as a 64-bit fixed-point fraction of a turn (24-bit mantissa times
+// the bits of 1 / 2 pi that matter, in integers), position times it wraps modulo one turn
 // by itself, and the 32 leading bits go to sincospif: off by at most 2^-24 half
-// turns (the rounding of that fraction to fp32) at any position.
+// turns (the rounding of that fraction to fp32) at any position and any finite inv_freq.
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -117,17 +117,32 @@ struct Raw8<float> {
   }
 };
 
-// inv_freq / 2 pi in units of 2^-64 turn, modulo one turn. x = m 2^e with a
-// 24-bit m; 1 / 2 pi = C 2^-64 with C to 62 significant bits.
+// 1 / 2 pi to 256 bits, leading word first (selected, not loaded: a table in memory
+// costs a call of one step 0.4 us).
+__device__ inline uint64_t inv_two_pi_word(int i) {
+  return i <= 0   ? 0x28be60db9391054aull
+         : i == 1 ? 0x7f09d5f47d4d3770ull
+         : i == 2 ? 0x36d8a5664f10e410ull
+                  : 0x7f9458eaf7aef158ull;
+}
+// 64 bits of 1 / 2 pi from bit `at` after the point on (zeros before the first), -64 <= at < 192.
+__device__ inline uint64_t inv_two_pi(int at) {
+  const int sh = at & 63;
+  const uint64_t hi = at < 0 ? 0 : inv_two_pi_word(at >> 6), lo = inv_two_pi_word((at >> 6) + 1);
+  return sh == 0 ? hi : (hi << sh) | (lo >> (64 - sh));
+}
+
+// inv_freq / 2 pi in units of 2^-64 turn, modulo one turn: x = m 2^e with a 24-bit m,
+// and whole turns of m times the bits of 2^e / 2 pi before the point drop out, so that
+// the 128 bits after it are enough for any finite x (Payne and Hanek's reduction).
+// Off by less than one unit: times a position, by at most 2^-33 turn.
 __device__ inline uint64_t turns_per_token(float x) {
-  constexpr uint64_t C = 2935890503282001226ull;  // floor(2^64 / (2 pi))
   const uint32_t u = __float_as_uint(x);
   const int be = (u >> 23) & 0xff;
   const uint32_t m = be == 0 ? (u & 0x7fffffu) : ((u & 0x7fffffu) | 0x800000u);
-  const int e = (be == 0 ? 1 : be) - 150;
-  const uint64_t hi = __umul64hi(static_cast<uint64_t>(m) << 40, C);  // m C 2^-24
-  const int sh = e + 24;
-  uint64_t f = sh <= -64 || sh >= 64 ? 0 : (sh < 0 ? hi >> -sh : hi << sh);
+  const int e = (be == 0 ? 1 : be) - 150;  // -149 .. 104 (not a number: 105, its angle is not used)
+  const uint64_t whole = e < -64 ? 0 : m * inv_two_pi(e);
+  const uint64_t f = whole + (e < -128 ? 0 : __umul64hi(m, inv_two_pi(e + 64)));
   return (u >> 31) ? 0 - f : f;
 }
 
