@@ -261,7 +261,8 @@ msa_status msa_select_topk_blocks_varlen(const void* q, int32_t num_q_heads, int
  * MSA_ERR_UNSUPPORTED otherwise); batch * Hkv <= 16384 units
  * (MSA_ERR_UNSUPPORTED above). out [batch, Hq, 128] in q's dtype; lse (nullable)
  * [batch, Hq] fp32 natural-log sum of exp(scale q.k).
- * An empty selection gives out = 0 and lse = -inf. */
+ * An empty selection gives out = 0 and lse = -inf; a NaN among a row's scores gives NaN
+ * in both (in a prefill alike). */
 msa_status msa_sparse_attn_decode(const void* q, int32_t num_q_heads, const msa_kv_desc* kv /* host */,
                                   const int32_t* idx, int32_t k_total, float scale, void* out,
                                   float* lse, void* ws, size_t ws_bytes, msa_stream_t stream);

@@ -228,6 +228,10 @@ __device__ inline void zero_tile_rows(uint8_t* tile, int box_stride, int first, 
   fence_proxy_async();
 }
 
+// Natural-log sum of exponentials of a row whose sum is l relative to the reference m (log2 units):
+// -inf marks a row that attends to nothing, and a NaN stays one.
+__device__ inline float lse_of(float m, float l) { return l == 0.f ? -INFINITY : m * kLn2 + logf(l); }
+
 __device__ inline float bf16_bits_to_f32(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 
 // Scores as order-preserving unsigned keys: a larger float gives a larger key.

@@ -165,6 +165,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_bf16_kernel(const __grid_c
       l0 += __shfl_xor_sync(0xffffffffu, l0, off);
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
+    // a NaN among the scores never moved m: keep it visible to the merge
+    if (l0 != l0) m0 = 0.f;
+    if (l1 != l1) m1 = 0.f;
   }
   pdl_trigger();    // the next kernel may start its set-up
   __syncthreads();  // every consumer is done with the ring: reuse it for the merge
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_f32_kernel(const float* __
 #pragma unroll
     for (int j = 0; j < kMaxGroup; ++j) {
       if (lane == 0) {
-        st.wm[warp][j] = m[j];
+        st.wm[warp][j] = l[j] != l[j] ? 0.f : m[j];  // as above
         st.wl[warp][j] = l[j];
       }
 #pragma unroll

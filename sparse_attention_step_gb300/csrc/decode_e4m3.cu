@@ -48,7 +48,7 @@ __device__ inline void e8_write(const DecodeArgs& a, int s, int h, int head, int
   const int64_t qrow = static_cast<int64_t>(s) * a.hq + h * a.grp + head;
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + qrow * kHeadDim + 4 * lane) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse != nullptr && lane == 0) a.lse[qrow] = L > 0.f ? M * kLn2 + logf(L) : -INFINITY;
+  if (a.lse != nullptr && lane == 0) a.lse[qrow] = lse_of(M, L);
 }
 // One head of a state of kPartFloats.
 __device__ inline void e8_store(float* part, int head, int lane, float M, float L, float4 acc) {

@@ -74,7 +74,7 @@ __device__ inline void write_final(const DecodeArgs& a, int s, int h, int head, 
   for (int i = 0; i < 8; ++i) x[i] = acc[i] * inv;
   const int64_t qrow = static_cast<int64_t>(s) * a.hq + h * a.grp + head;
   store_out8<T>(reinterpret_cast<T*>(a.out) + qrow * kHeadDim + d0, x);
-  if (a.lse != nullptr && d0 == 0) a.lse[qrow] = (L > 0.f) ? (M * kLn2 + logf(L)) : -INFINITY;
+  if (a.lse != nullptr && d0 == 0) a.lse[qrow] = lse_of(M, L);
 }
 
 // The CTA-level tail shared by both paths: merge the consumer warps' states

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kPfThreads) prefill_bf16_kernel(const __grid_c
     for (int dt = 0; dt < 16; ++dt) {
       *reinterpret_cast<uint32_t*>(dst + 8 * dt) = pack_bf16(o[dt][2 * hr] * inv, o[dt][2 * hr + 1] * inv);
     }
-    if (a.lse != nullptr && c == 0) a.lse[qrow[hr]] = l[hr] > 0.f ? m[hr] * kLn2 + logf(l[hr]) : -INFINITY;
+    if (a.lse != nullptr && c == 0) a.lse[qrow[hr]] = lse_of(m[hr], l[hr]);
   }
 }
 

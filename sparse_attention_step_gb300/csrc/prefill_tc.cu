@@ -907,7 +907,7 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
       }
     }
     if (live && hf == 0 && a.lse != nullptr)
-      a.lse[tq * a.hq + head] = (L > 0.f) ? (m * kLn2 + logf(L)) : -INFINITY;
+      a.lse[tq * a.hq + head] = lse_of(m, L);
   }
   tc::fence_before();
   __syncthreads();

@@ -589,6 +589,9 @@ __global__ void __launch_bounds__(kStThreads, 2) decode_step_kernel(const __grid
       l0 += __shfl_xor_sync(0xffffffffu, l0, off);
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
+    // a NaN among the scores never moved m: keep it visible to the merge
+    if (l0 != l0) m0 = 0.f;
+    if (l1 != l1) m1 = 0.f;
   } else if (warp > kStAttnWarps && rank == 0) {
     // warps 5-7 of the leader: the unit's list, ascending (block 0 when kept as
     // the sink, the kk selected blocks by counting -- each one's position is
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kStThreads, 2) decode_step_kernel(const __grid
         v.w = pack_bf16(acc[6] * inv, acc[7] * inv);
         const int64_t qrow = static_cast<int64_t>(s) * a.hq + h * a.grp + head;
         *reinterpret_cast<uint4*>(a.out + qrow * kHeadDim + d0) = v;
-        if (a.lse != nullptr && d0 == 0) a.lse[qrow] = L > 0.f ? M * kLn2 + logf(L) : -INFINITY;
+        if (a.lse != nullptr && d0 == 0) a.lse[qrow] = lse_of(M, L);
       } else {
         // push this CTA's part of piece `tid` (head, 8 dims) to the piece's
         // owner, rank tid % C: slot [rank][tid / C] of the owner's receive
@@ -759,7 +762,7 @@ __global__ void __launch_bounds__(kStThreads, 2) decode_step_kernel(const __grid
       w.w = pack_bf16(v[7] * inv, v[8] * inv);
       const int64_t qrow = static_cast<int64_t>(s) * a.hq + h * a.grp + head;
       *reinterpret_cast<uint4*>(a.out + qrow * kHeadDim + d0) = w;
-      if (a.lse != nullptr && d0 == 0) a.lse[qrow] = v[0] > 0.f ? Mx * kLn2 + logf(v[0]) : -INFINITY;
+      if (a.lse != nullptr && d0 == 0) a.lse[qrow] = lse_of(Mx, v[0]);
     }
   }
 }
