@@ -208,7 +208,7 @@ msa_status msa_pool_block_keys(const msa_kv_desc* kv /* host */, int64_t first_b
  * candidates by (score descending, block ascending) plus the forced block are
  * written sorted ascending, padded with -1;
  * k_total >= min(k_scored, max_blocks) + the number of kept blocks (bits of
- * force_local). With the sink bit, block 0 leads the list and the candidates
+ * force_local), and, as in every call with lists, <= 2^30 (MSA_ERR_UNSUPPORTED above). With the sink bit, block 0 leads the list and the candidates
  * start at block 1.
  * scores_out (nullable): [units, max_blocks] fp32 raw scores of the candidate
  * blocks (max_blocks = max_tokens/64 or max_pages_per_seq); other entries are

@@ -133,6 +133,9 @@ msa_status make_q_map(CUtensorMap* map, const void* base, int64_t n_tokens, int 
 // 16-byte aligned.
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Entries of a list: a kernel's walk over one counts in 32 bits, past its end by up to a stride.
+constexpr int32_t kMaxListLen = 1 << 30;
+
 // Arrays of 4- and 8-byte elements at their natural alignment (null passes).
 template <typename... P>
 bool aligned_to(uintptr_t bytes, P... p) {
@@ -281,6 +284,7 @@ msa_status decode_common(const void* q, int hq, const msa_kv_desc* kv, const int
   if ((st = check_q_heads(kv, hq)) != MSA_OK) return st;
   if (q == nullptr || out == nullptr) return MSA_ERR_INVALID_ARG;
   if (idx != nullptr && k_total <= 0) return MSA_ERR_INVALID_ARG;
+  if (k_total > kMaxListLen) return MSA_ERR_UNSUPPORTED;
   if (!(scale > 0.f)) return MSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return MSA_ERR_INVALID_ARG;
   if (!decode_units_fit(kv)) return MSA_ERR_UNSUPPORTED;
@@ -335,6 +339,7 @@ msa_status prefill_common(const void* q, int hq, const PrefillBatch& pb, int64_t
   if ((st = check_q_heads(kv, hq)) != MSA_OK) return st;
   if (q == nullptr || out == nullptr) return MSA_ERR_INVALID_ARG;
   if (idx != nullptr && k_total <= 0) return MSA_ERR_INVALID_ARG;
+  if (k_total > kMaxListLen) return MSA_ERR_UNSUPPORTED;
   if (!(scale > 0.f)) return MSA_ERR_INVALID_ARG;
   if (kv->dtype == MSA_DTYPE_F32) return MSA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(out)) return MSA_ERR_INVALID_ARG;
@@ -444,6 +449,7 @@ msa_status check_select(const void* q, int32_t num_q_heads, const void* pooled, 
   if ((st = check_q_heads(kv, num_q_heads)) != MSA_OK) return st;
   if (cfg->mode != MSA_SCORE_MEAN_POOLED_KEYS && cfg->mode != MSA_SCORE_TOKEN_MAX) return MSA_ERR_UNSUPPORTED;
   if (cfg->k_scored < 0 || k_total <= 0) return MSA_ERR_INVALID_ARG;
+  if (k_total > kMaxListLen) return MSA_ERR_UNSUPPORTED;
   if (k_total < std::min<int64_t>(cfg->k_scored, kv_max_blocks(kv)) + forced_count(cfg))
     return MSA_ERR_INVALID_ARG;
   if (cfg->force_local < 0 || cfg->force_local > (kForceLocal | kForceSink)) return MSA_ERR_INVALID_ARG;
@@ -628,7 +634,7 @@ msa_status decode_step_common(const void* q, int32_t num_q_heads, const void* po
   if (cfg == nullptr || q == nullptr || pooled == nullptr || idx_out == nullptr || out == nullptr)
     return MSA_ERR_INVALID_ARG;
   if ((st = check_q_heads(kv, num_q_heads)) != MSA_OK) return st;
-  if (cfg->q_tile != 1) return MSA_ERR_UNSUPPORTED;
+  if (cfg->q_tile != 1 || k_total > kMaxListLen) return MSA_ERR_UNSUPPORTED;
   if (!(scale > 0.f)) return MSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(pooled)) return MSA_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
@@ -907,6 +913,7 @@ extern "C" msa_status msa_sparse_attn_decode_noalloc(const void* q, int32_t num_
   if (st != MSA_OK) return st;
   if ((st = check_q_heads(kv, num_q_heads)) != MSA_OK) return st;
   if (q == nullptr || out == nullptr || idx == nullptr || k_total <= 0) return MSA_ERR_INVALID_ARG;
+  if (k_total > kMaxListLen) return MSA_ERR_UNSUPPORTED;
   if (!(scale > 0.f)) return MSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return MSA_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;

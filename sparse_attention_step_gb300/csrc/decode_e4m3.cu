@@ -181,7 +181,7 @@ constexpr size_t kE8StreamBytes =
 
 // CTAs with a run: kE8MinRun positions or more each, as long as there are that many.
 __device__ inline int e8_runs(int T) {
-  return min(static_cast<int>(gridDim.x), (T + kE8MinRun - 1) / kE8MinRun);
+  return min(static_cast<int>(gridDim.x), T / kE8MinRun + (T % kE8MinRun != 0 ? 1 : 0));  // T may be 2^31 - 2
 }
 // Positions [0, T) dealt to n <= T CTAs: the first T % n get one more.
 struct E8Deal {
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kE8Threads, 2)
     if (a.lse != nullptr)
       for (int i = tid; i < a.hq; i += kE8Threads) a.lse[static_cast<int64_t>(s) * a.hq + i] = -INFINITY;
   }
-  if (blockIdx.x >= e8_runs(T)) return;
+  if (static_cast<int>(blockIdx.x) >= e8_runs(T)) return;
   const int hi = deal.first(blockIdx.x + 1);
   u.s = s0;
   u.load(kv, a);
