@@ -282,7 +282,8 @@ msa_status msa_sparse_attn_decode(const void* q, int32_t num_q_heads, const msa_
  * e4m3: the weight of a token (its softmax weight times its V scale) is rounded to 11
  * bits, or, where it is small against the row's largest, to a multiple of a fixed fraction of
  * that, such that the roundings of all small weights of a row add up to at most 2^-12 of the
- * largest (rows of up to 2^28 tokens). For every cache type the output is summed in fp32 on
+ * largest (rows of up to 2^28 tokens); V scales may be as large as 2^80 (where a larger one leaves
+ * a row's sum too small to be sure of, the device status records MSA_ERR_UNSUPPORTED). For every cache type the output is summed in fp32 on
  * the tensor cores, where a token whose share of a dim is below 2^-23 of that dim's sum so far
  * may be cut off.
  * out [n_q_tokens, Hq, 128] KV dtype (e4m3: bf16); lse (nullable) [n_q_tokens, Hq] fp32. */

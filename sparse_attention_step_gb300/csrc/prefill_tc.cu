@@ -141,6 +141,10 @@ __device__ inline float weight_room(int nblk) {
 constexpr float kWeightTop = 32768.f;
 constexpr float kSumBits = 90.f;           // l: at most 2^90 a term at a new reference,
 constexpr float kSumTop = 1.26765060e30f;  // 2^100 a block after
+// l's terms lie as far below 2^0 as V's scales lift the reference above the scores, and vanish below 2^-126: a
+// sum below 2^-81 (a V scale above 2^80) may have lost too many.
+constexpr float kSumLeast = 4.1359030627651384e-25f;
+constexpr float kRefTop = 16777216.f;  // (no reference yet, or scores that fp32 does not hold to a bit: nothing to tell)
 constexpr size_t kTcE8Smem = kTcSmem + kCodeSlots * kE8Tile + ((sizeof(E8Tail) + 15) / 16) * 16;
 static_assert(kTcE8Smem <= 232448, "shared memory of a CTA");
 
@@ -905,6 +909,9 @@ __global__ void __launch_bounds__(kE8 ? kTcE8Threads : kTcThreads, 1)
           gdst[qq] = *reinterpret_cast<const uint4*>(ob + row * 256 + ((c ^ (row & 7)) << 4));
         }
       }
+    }
+    if constexpr (kE8) {
+      if (live && L < kSumLeast && fabsf(m) < kRefTop) set_status(a.status, MSA_ERR_UNSUPPORTED, kIdPrefill);
     }
     if (live && hf == 0 && a.lse != nullptr)
       a.lse[tq * a.hq + head] = lse_of(m, L);
