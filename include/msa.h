@@ -394,7 +394,8 @@ msa_status msa_sparse_attn_decode_noalloc(const void* q, int32_t num_q_heads, co
  *  - seq_lens_out[s] = n_s + q_counts[s].
  *  - q_off [batch + 1]: the first row of each sequence's new tokens, which lie
  *    back to back: token r of s is row q_off[s] + r; q_off[batch] is their
- *    number.
+ *    number. The decode calls take row s of q for sequence s: with one token each
+ *    these rows are that; otherwise gather the rows q_off[s + 1] - 1.
  *  - positions [n_slots] int32: n_s + r for that row; slots [n_slots] int64: its
  *    cache slot, page * 64 + offset (paged) or s * max_tokens + position
  *    (contiguous), what msa_qk_norm_rope_append takes. n_slots is the row count
@@ -425,7 +426,7 @@ msa_status msa_extend_sequences(const msa_kv_desc* kv /* host */, const int32_t*
  * ascending, are pushed on the stack: the j-th to free_pages[*free_count + j];
  * *free_count_out is the new height. Pages must belong to one sequence
  * only (a shared one would be pushed twice). The page table is left as it is:
- * its entries past a sequence's length are not read by any call. In place use
+ * its entries past a sequence's length (or its chunk's end) are not read by any call. In place use
  * and contiguous caches as for msa_extend_sequences; batch <= 8192.
  * All or nothing: a negative value, a length past the capacity, or a stack
  * that would exceed num_pages entries sets MSA_ERR_DEVICE_BOUNDS, lengths and

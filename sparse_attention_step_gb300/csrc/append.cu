@@ -21,10 +21,10 @@
 // tokens on their way), which leaves the registers to eight CTAs an SM. All of
 // it is fp32, two elements an instruction (f32x2); the output type's rounding is the
 // only one.
-// 8192 tokens x (64 + 16) heads, bf16, pages in random order: 57.6 us, 5.83 TB/s (a
+// 8192 tokens x (64 + 16) heads, bf16, pages in random order: 58.0 us, 5.79 TB/s (a
 // plain copy of the same bytes: 50.5). Steps: angles a lane, rows in registers,
 // two tokens' heads in unequal runs 74 us; CTAs of equal runs, angles shared 64;
-// the ring 58. It stays short of the copy by its instructions (half of the issue
+// the ring 57.6, angles exact for any inv_freq 58.0. It stays short of the copy by its instructions (half of the issue
 // slots) and its stores of single rows.
 //
 // Angles: fp32 products lose a far token's angle (at position 2^20 an fp32

@@ -6,9 +6,9 @@
 // (scores in log2 units). Codes go to the tensor cores as fp16, which holds
 // every e4m3 value exactly; a row's scale never touches its codes: K's
 // multiplies the fp32 score, V's joins the exponent of the weight, so a weight is
-// one exp2 and lies in (0, 1] whatever the sizes of the rows. M is the largest
-// s_t + log2 vs_t seen, m the largest s_t: two references, because a row that
-// decides l need not decide O.
+// one exp2 and lies below 2^kWeightGrow whatever the sizes of the rows. M is the largest
+// s_t + log2 vs_t seen when it last moved, m the same of s_t (they move once a token passes them
+// by kWeightGrow or kSumGrow): two references, because a row that decides l need not decide O.
 //
 // Rounding: a query head is scaled by a power of two to below 1 and kept in
 // fp16 (11 bits: a bf16 query is exact down to 2^-16 of the head's largest element,

@@ -41,16 +41,19 @@
 // below 1 and turned into fp16 in place, once, by the softmax warps. Scales never
 // touch the tiles: a score is multiplied by its key's K scale, and the weight, after
 // it is summed, by its key's V scale, both in fp32. A row keeps one reference R,
-// near the largest score plus log2 |V's scale|: weights go to fp16 as 2^(x - R) vs,
+// near the largest score plus log2 |V's scale| (below it by the room that long rows need,
+// weight_room): weights go to fp16 as 2^(x - R) vs,
 // l sums 2^(x - R), which fp32 holds whatever the scales. No maximum is taken
 // unless it is needed: the sum of the weights before their scales, times the
 // block's largest |V scale|, bounds them. Rows past the chunk's end are widened
-// to zeros, their scales are staged as zeros and their scores masked.
+// to zeros, their scales are staged as zeros and their scores masked. (bf16 caches: zeros
+// follow the V tile of the block in which the chunk ends, by a bulk copy: 507 -> 511 us; cleared by
+// the softmax or the MMA warp 524 and 586.)
 // Registers: 6 warpgroups x 80 are split by setmaxnreg into 4 (softmax) x 88 + 2 x
 // 64, where nothing spills. Groups below 8 leave rows idle: a token's rows are 4 (G <=
 // 4, a tile's 64 tokens in one CTA) or 8. 8192 tokens on a prefix of 131072, 33 blocks a
-// tile, 64 / 8 heads: 736 us, 759 TFLOP/s (bf16 cache 507); 56 / 8: 734; 32 / 8: 372.
-// Where scores spread over tens of bits, so that most pairs move a reference, 1183.
+// tile, 64 / 8 heads: 737 us, 757 TFLOP/s (bf16 cache 511); 56 / 8: 736; 32 / 8: 374.
+// Where scores spread over tens of bits, so that most pairs move a reference, 1227.
 // The steps, 64 / 8 heads: mma.sync on fp16 tiles 3602 (56 / 8: 2907 in its last form; slower
 // at every size and group, so it is not kept); bf16 tiles here with V's scales in bf16
 // weights 1366; the maxima of every pair taken and 104 + 32 registers 847; maxima as

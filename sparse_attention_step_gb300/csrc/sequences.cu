@@ -1,6 +1,7 @@
 // Where the tokens of a step go: sequences grow (pages popped off a stack of
 // free pages, positions and cache slots of the new tokens) and shrink (pages
-// pushed back), on the GPU, from lengths and counts that never visit the host.
+// pushed back), on the GPU, from lengths and counts in its memory: a step of single tokens never
+// takes them to the host (a batch of prefill chunks does: those calls take starts and counts there).
 //
 // With n_s the length of sequence s, c_s its new tokens and B = 64 tokens a
 // block:
